@@ -27,16 +27,16 @@ DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 def listed():
     return [
         # a handful of chats, one new token each: launch latency is all there is
-        dict(name="rope_tiny_step", op="rope", tokens=4, chats=4, hq=4, hkv=2, d=64, dtype="f16", rotary=64,
+        dict(name="rope_tiny_step", op="rope", tokens=4, hq=4, hkv=2, d=64, dtype="f16", rotary=64,
              interleaved=False, norm=False, yarn=1.0, fp8=False, fused=False, padded=0, far=2048),
         # the decode step of a full batch at the 70B shape, padded as for a captured graph, normed heads
-        dict(name="rope_step_70b", op="rope", tokens=256, chats=256, hq=64, hkv=8, d=128, dtype="bf16", rotary=128,
+        dict(name="rope_step_70b", op="rope", tokens=256, hq=64, hkv=8, d=128, dtype="bf16", rotary=128,
              interleaved=False, norm=True, yarn=1.0, fp8=False, fused=True, padded=11, far=34000),
         # one piece of a long prompt with 20 decode tokens, rotation scaled for a long context
-        dict(name="rope_piece_70b", op="rope", tokens=3770, chats=20, hq=64, hkv=8, d=128, dtype="bf16", rotary=128,
+        dict(name="rope_piece_70b", op="rope", tokens=3770, hq=64, hkv=8, d=128, dtype="bf16", rotary=128,
              interleaved=True, norm=False, yarn=8.0, fp8=False, fused=True, padded=0, far=30000),
         # a whole 30,000-token prompt into an E4M3 cache, half of each head rotated
-        dict(name="rope_prompt_fp8", op="rope", tokens=30000, chats=0, hq=64, hkv=8, d=128, dtype="bf16", rotary=64,
+        dict(name="rope_prompt_fp8", op="rope", tokens=30000, hq=64, hkv=8, d=128, dtype="bf16", rotary=64,
              interleaved=False, norm=True, yarn=1.0, fp8=True, fused=False, padded=0, far=30000),
         # a few chats with small trees
         dict(name="plan_few", op="plan", seqs=4, nodes=8, words=1, far=2048),
@@ -79,8 +79,7 @@ def draw(rng):
     hq = hkv * rng.choice([1, 2, 4, 8])
     if op == "rope":
         fp8 = d == 128 and rng.random() < 0.4
-        tokens = _log(rng, 1, 8000)
-        return dict(op=op, tokens=tokens, chats=min(tokens, rng.choice([0, 20, 256])), hq=hq, hkv=hkv, d=d, dtype=dtype,
+        return dict(op=op, tokens=_log(rng, 1, 8000), hq=hq, hkv=hkv, d=d, dtype=dtype,
                     rotary=16 * rng.randint(1, d // 16), interleaved=rng.random() < 0.5, norm=rng.random() < 0.5,
                     yarn=rng.choice([1.0, 4.0, 8.0]), fp8=fp8, fused=rng.random() < 0.5, padded=rng.randint(0, 5),
                     far=_log(rng, 16, 1000000))
@@ -174,15 +173,9 @@ def prepare(case, seed):
         s["q"], s["k"], s["v"] = qkv.split([hq, hkv, hkv], dim=1)
         if not case["fused"]:
             s["q"], s["k"], s["v"] = (x.contiguous() for x in (s["q"], s["k"], s["v"]))
-        # a prompt's piece from within a page on, then the tokens of chats, each in a page of its own
-        chats, start = case["chats"], int(r.integers(0, case["far"]))
-        piece = start + np.arange(t - chats)
-        s["positions"] = _dev(np.concatenate([piece, r.integers(0, case["far"], chats)]).astype(np.int32))
-        pages = (t - chats) // BLOCK + 2
-        pool = (pages + chats) * 5 // 4
-        ids = r.permutation(pool).astype(np.int64)
-        slots = np.concatenate([ids[piece // BLOCK - start // BLOCK] * BLOCK + piece % BLOCK,
-                                ids[pages:pages + chats] * BLOCK + r.integers(0, BLOCK, chats)])
+        s["positions"] = _dev(r.integers(0, case["far"], t).astype(np.int32))
+        pool = (t + BLOCK - 1) // BLOCK * 5 // 4 + 1
+        slots = r.permutation(pool * BLOCK)[:t].astype(np.int64)
         if case["padded"]:
             slots[-min(t, case["padded"]):] = -1
         s["slots"] = _dev(slots)
