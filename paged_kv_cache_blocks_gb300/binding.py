@@ -441,8 +441,9 @@ def _rope(call, q, k, v, positions, slot_mapping, inv_freq, scales, k_cache, v_c
     strides = []
     for x in (q, k, v):
         st, sh, sd = x.stride()
-        if x.get_device() != d or sd != 1 or (sh != D and x.shape[1] > 1):
-            raise ValueError("q, k and v must be CUDA tensors whose heads are contiguous (any token stride)")
+        # a token stride of 0 (one row for all tokens) means packed to the library
+        if x.get_device() != d or sd != 1 or (sh != D and x.shape[1] > 1) or (st == 0 and T > 1):
+            raise ValueError("q, k and v must be CUDA tensors whose heads are contiguous (any token stride but 0)")
         strides.append(st if T > 1 else 0)   # a lone token's stride means nothing (and may be anything)
     if not (k.shape == v.shape == (T, H, D) and k.dtype == v.dtype == qt):
         raise TypeError("k and v must be [tokens, kv heads, head_dim] of q's dtype")
@@ -479,8 +480,8 @@ def pa_rope_cache_write(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_c
                         k_norm=None, eps=1e-6, interleaved=False, attn_factor=1.0, dtype=None, stream=None):
     """Norm (optional), rotate q and k by their positions, write k and v to the cache; returns q [T, Hq, D].
 
-    q [T, Hq, D], k and v [T, Hkv, D]: contiguous heads, any token stride, so
-    views of one projection's rows do.  positions [T] int32; slot_mapping [T]
+    q [T, Hq, D], k and v [T, Hkv, D]: contiguous heads, any token stride but
+    0, so views of one projection's rows do.  positions [T] int32; slot_mapping [T]
     int64 (< 0: padding); inv_freq [rotary_dim / 2] float64; caches
     [NB, Hkv, 16, D].  ``out`` may be a contiguous q itself.
     """

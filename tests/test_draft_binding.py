@@ -1,0 +1,75 @@
+"""The binding's checks of the rotation, draft trees and compaction, on the
+CPU: a recorder stands in for the library, so a call that passes the checks
+shows what would have reached the kernels, and nothing runs."""
+import types
+
+import pytest
+import torch
+
+
+class Recorder:
+    """libpa's device calls: each records its arguments and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.calls.append((name, a))
+            return 0
+        call.__name__ = name
+        return call
+
+    def pa_decode_tree_workspace_bytes(self, *a):
+        return 4096
+
+
+@pytest.fixture
+def pa(monkeypatch):
+    from paged_kv_cache_blocks_gb300 import binding
+
+    def here(*ts):
+        if not all(t.is_contiguous() for t in ts):
+            raise ValueError("not contiguous")
+
+    rec = Recorder()
+    monkeypatch.setattr(binding, "lib", lambda: rec)
+    monkeypatch.setattr(binding, "_need_here", here)
+    monkeypatch.setattr(binding, "_stream", lambda stream: None)
+    return types.SimpleNamespace(binding=binding, calls=rec.calls)
+
+
+def rope_args(T=6, hq=4, hkv=2, D=128, dtype=torch.float16):
+    z = lambda *s: torch.zeros(*s, dtype=dtype)
+    return dict(q=z(T, hq, D), k=z(T, hkv, D), v=z(T, hkv, D), positions=torch.zeros(T, dtype=torch.int32),
+                slot_mapping=torch.zeros(T, dtype=torch.int64), inv_freq=torch.zeros(D // 2, dtype=torch.float64),
+                k_cache=z(3, hkv, 16, D), v_cache=z(3, hkv, 16, D))
+
+
+def e4m3_args(T=6, hq=4, hkv=2):
+    a = rope_args(T, hq, hkv)
+    a.pop("k_cache"), a.pop("v_cache")
+    return a | dict(k_scale=torch.ones(hkv), v_scale=torch.ones(hkv),
+                    k_cache8=torch.zeros(3, hkv, 16, 128, dtype=torch.uint8),
+                    v_cache8=torch.zeros(3, hkv, 128, 16, dtype=torch.uint8))
+
+
+def test_rope_calls_pass(pa):
+    pa.binding.pa_rope_cache_write(**rope_args())
+    pa.binding.pa_rope_cache_write_fp8(**e4m3_args())
+    assert [c[0] for c in pa.calls] == ["pa_rope_cache_write", "pa_rope_cache_write_fp8"]
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_rope_refuses_one_row_repeated_over_the_tokens(pa, name):
+    """Token stride 0 means "packed" to the library: it would read T rows of a tensor that holds one."""
+    for call, a in ((pa.binding.pa_rope_cache_write, rope_args()), (pa.binding.pa_rope_cache_write_fp8, e4m3_args())):
+        a[name] = a[name][:1].expand(6, -1, -1)
+        assert a[name].stride(0) == 0
+        with pytest.raises(ValueError):
+            call(**a)
+    assert not pa.calls
+    a = rope_args(T=1)
+    a[name] = a[name].as_strided(a[name].shape, (0, 128, 1))      # one token: its stride means nothing
+    pa.binding.pa_rope_cache_write(**a)
+    assert len(pa.calls) == 1
