@@ -455,10 +455,12 @@ def _rope(call, q, k, v, positions, slot_mapping, inv_freq, scales, k_cache, v_c
     for w in norms:
         if w.dtype != qt or w.numel() != D:
             raise TypeError("norm weights must be [head_dim] of q's dtype")
-    NB, KH, rows, KD = k_cache.shape
-    if not (KH == H and NB * KH * rows * KD == v_cache.numel() == NB * H * BLOCK_SIZE * D
+    NB = k_cache.shape[0]
+    if not (k_cache.shape == (NB, H, BLOCK_SIZE, D)
+            and v_cache.shape == ((NB, H, D, BLOCK_SIZE) if scales else (NB, H, BLOCK_SIZE, D))
             and (scales or _same_16bit(q, k_cache, v_cache))):
-        raise TypeError("caches must be [blocks, kv heads, 16, head_dim] of q's dtype")
+        raise TypeError("caches must be [blocks, kv heads, 16, head_dim] of q's dtype (E4M3: V [blocks, kv heads, "
+                        "head_dim, 16])")
     code = _dtype_code(q, dtype)
     if out is None:
         out = _empty((T, Hq, D), qt, q, stream)

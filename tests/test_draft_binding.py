@@ -73,3 +73,18 @@ def test_rope_refuses_one_row_repeated_over_the_tokens(pa, name):
     a[name] = a[name].as_strided(a[name].shape, (0, 128, 1))      # one token: its stride means nothing
     pa.binding.pa_rope_cache_write(**a)
     assert len(pa.calls) == 1
+
+
+def test_rope_refuses_caches_of_another_layout(pa):
+    """As many elements, but rows and dimensions the other way round."""
+    for name in ("k_cache", "v_cache"):
+        a = rope_args()
+        a[name] = torch.zeros(3, 2, 128, 16, dtype=torch.float16)
+        with pytest.raises(TypeError):
+            pa.binding.pa_rope_cache_write(**a)
+    for name, shape in (("k_cache8", (3, 2, 128, 16)), ("v_cache8", (3, 2, 16, 128)), ("v_cache8", (2, 3, 128, 16))):
+        a = e4m3_args()
+        a[name] = torch.zeros(*shape, dtype=torch.uint8)
+        with pytest.raises(TypeError):
+            pa.binding.pa_rope_cache_write_fp8(**a)
+    assert not pa.calls
