@@ -193,9 +193,9 @@ def _need_here(first, *others):
 
 
 def _same_16bit(q, k_cache, v_cache):
-    """Whether the caches hold q's element type (int16 tensors are bit patterns of either)."""
+    """Whether q and the caches hold one 16-bit element type (int16 tensors are bit patterns of either)."""
     qt, ct = q.dtype, k_cache.dtype
-    return ct == v_cache.dtype and (ct == qt or ct == torch.int16 or qt == torch.int16) and k_cache.element_size() == 2
+    return ct == v_cache.dtype and (ct == qt or ct == torch.int16 or qt == torch.int16) and ct.itemsize == qt.itemsize == 2
 
 
 def _need(cond, what):
@@ -445,8 +445,8 @@ def _rope(call, q, k, v, positions, slot_mapping, inv_freq, scales, k_cache, v_c
         if x.get_device() != d or sd != 1 or (sh != D and x.shape[1] > 1) or (st == 0 and T > 1):
             raise ValueError("q, k and v must be CUDA tensors whose heads are contiguous (any token stride but 0)")
         strides.append(st if T > 1 else 0)   # a lone token's stride means nothing (and may be anything)
-    if not (k.shape == v.shape == (T, H, D) and k.dtype == v.dtype == qt):
-        raise TypeError("k and v must be [tokens, kv heads, head_dim] of q's dtype")
+    if not (k.shape == v.shape == (T, H, D) and k.dtype == v.dtype == qt and qt.itemsize == 2):
+        raise TypeError("k and v must be [tokens, kv heads, head_dim] of q's dtype, a 16-bit one")
     if not (positions.dtype == torch.int32 and slot_mapping.dtype == torch.int64
             and positions.numel() == slot_mapping.numel() == T):
         raise TypeError("positions must be int32 and slot_mapping int64, one entry per token")

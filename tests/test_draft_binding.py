@@ -88,3 +88,27 @@ def test_rope_refuses_caches_of_another_layout(pa):
         with pytest.raises(TypeError):
             pa.binding.pa_rope_cache_write_fp8(**a)
     assert not pa.calls
+
+
+def tree_args(T=6, hq=4, hkv=2, D=128, dtype=torch.float16):
+    z = lambda *s: torch.zeros(*s, dtype=dtype)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    return dict(q=z(T, hq, D), k_cache=z(3, hkv, 16, D), v_cache=z(3, hkv, 16, D), block_tables=i(2, 4),
+                seq_lens=i(2), q_offsets=i(3), masks=torch.zeros(T, 1, dtype=torch.int64), scale=0.1)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.float32, torch.float64])
+def test_q_that_is_not_16_bit_is_refused(pa, dtype):
+    """Beside bit-pattern caches q's element type was not looked at: a one-byte q is half as long as what is read."""
+    bits = dict(k_cache=torch.zeros(3, 2, 16, 128, dtype=torch.int16), v_cache=torch.zeros(3, 2, 16, 128, dtype=torch.int16))
+    with pytest.raises(TypeError):
+        pa.binding.pa_decode_tree(**(tree_args() | bits | dict(q=torch.zeros(6, 4, 128, dtype=dtype))), dtype="f16")
+    with pytest.raises(TypeError):
+        pa.binding.pa_rope_cache_write(**(rope_args(dtype=dtype) | bits), dtype="f16")
+    a = {k: v.to(dtype) if k in ("q", "k", "v") else v for k, v in e4m3_args().items()}
+    with pytest.raises(TypeError):
+        pa.binding.pa_rope_cache_write_fp8(**a, dtype="f16")
+    assert not pa.calls
+    pa.binding.pa_decode_tree(**(tree_args() | bits), dtype="f16")
+    pa.binding.pa_decode_tree(**(tree_args(dtype=torch.int16)), dtype="bf16")
+    assert len(pa.calls) == 2
