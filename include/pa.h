@@ -542,7 +542,9 @@ int pa_decode_tree(const void* d_q, const void* d_k_cache, const void* d_v_cache
  * pa_seq_truncate.
  *   k_caches, v_caches   host arrays of num_layers device pointers, each
  *                        [num_blocks][num_kv_heads][16][head_dim], 16-bit;
- *                        num_blocks * num_kv_heads * 16 < 2^31
+ *                        num_blocks * num_kv_heads * 16 < 2^31.  No two of
+ *                        them may share memory (PA_ERR_INVALID): a layer named
+ *                        twice would have its rows moved twice
  *   d_block_tables, d_seq_lens, d_q_offsets  as the trees were decoded with
  *   d_accepted           [num_seqs][max_accepted] int32, ascending per sequence
  *                        (a path from a root down is)

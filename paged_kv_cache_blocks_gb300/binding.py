@@ -608,7 +608,7 @@ def pa_cache_compact(k_caches, v_caches, block_tables, seq_lens, q_offsets, acce
     """Move the accepted tokens of each draft tree to the tree's first places, in every layer; returns the new lengths.
 
     k_caches, v_caches: one tensor [layers, NB, Hkv, 16, D] each, or lists of
-    [NB, Hkv, 16, D] tensors; accepted [B, most] int32, ascending per
+    [NB, Hkv, 16, D] tensors, each named once; accepted [B, most] int32, ascending per
     sequence; num_accepted [B] int32.
     """
     _need_here(block_tables, seq_lens, q_offsets, accepted, num_accepted)

@@ -669,6 +669,31 @@ int pa_decode_tree(const void* d_q, const void* d_k_cache, const void* d_v_cache
   return rc ? fail(rc, why) : PA_OK;
 }
 
+namespace {
+
+// Whether any two of the n + n caches of `bytes` bytes overlap.  Layers lie in
+// ascending order as a rule, and are then walked once.
+bool caches_overlap(void* const* k, void* const* v, int32_t n, uint64_t bytes) {
+  auto at = [&](int32_t i) { return reinterpret_cast<uintptr_t>(i < n ? k[i] : v[i - n]); };
+  bool ascending = true;
+  for (int32_t i = 1; i < n; ++i) ascending = ascending && k[i] > k[i - 1] && v[i] > v[i - 1];
+  if (ascending) {
+    uintptr_t end = 0;
+    for (int32_t i = 0, j = 0; i + j < 2 * n;) {
+      const uintptr_t x = j == n || (i < n && at(i) < at(n + j)) ? at(i++) : at(n + j++);
+      if (x < end) return true;
+      end = x + bytes;
+    }
+    return false;
+  }
+  for (int32_t i = 0; i < 2 * n; ++i)
+    for (int32_t j = 0; j < i; ++j)
+      if (at(i) < at(j) + bytes && at(j) < at(i) + bytes) return true;
+  return false;
+}
+
+}  // namespace
+
 int pa_cache_compact(void* const* k_caches, void* const* v_caches, int32_t num_layers, int64_t num_blocks,
                      int32_t num_kv_heads, int32_t head_dim, const int32_t* d_block_tables,
                      int32_t max_blocks_per_seq, const int32_t* d_seq_lens, const int32_t* d_q_offsets,
@@ -694,6 +719,10 @@ int pa_cache_compact(void* const* k_caches, void* const* v_caches, int32_t num_l
   for (int32_t i = 0; i < num_layers; ++i)
     if (!k_caches[i] || !v_caches[i] || !aligned(k_caches[i], 16) || !aligned(v_caches[i], 16))
       return fail(PA_ERR_INVALID, "pa_cache_compact: every layer's caches must be 16-byte aligned device memory");
+  if (num_layers > INT32_MAX / 2 ||
+      caches_overlap(k_caches, v_caches, num_layers,
+                     static_cast<uint64_t>(num_blocks) * num_kv_heads * PA_BLOCK_SIZE * head_dim * 2))
+    return fail(PA_ERR_INVALID, "pa_cache_compact: no two caches may share memory (their rows would move twice)");
   if (!aligned(d_block_tables, 4) || !aligned(d_seq_lens, 4) || !aligned(d_q_offsets, 4) ||
       !aligned(d_accepted, 4) || !aligned(d_num_accepted, 4) || !aligned(d_new_seq_lens, 4) ||
       !aligned(d_error_bits, 4))

@@ -197,3 +197,17 @@ def test_speculative_steps_as_they_would_be_used(pa, hq, hkv, D, dt):
         for t in range(n):
             at = (slice(None), tab[b][t // 16], slice(None), t % 16)
             assert torch.equal(kc[at], plain_k[at]) and torch.equal(vc[at], plain_v[at])
+
+
+def test_layers_in_any_order_and_interleaved(pa):
+    """K and V of a layer beside each other in one buffer, and the layers named last to first."""
+    c, table, lens, off, acc, num = make(8, [20, 33], [9, 9], [5, 4], 3, 2, 64, "f16")
+    both = torch.from_numpy(np.stack(c, 1)).cuda().view(torch.float16)      # [layers, K / V, ...]
+    want, _ = ref.compact(c, table, lens, off, acc, num)
+    a = [dev(x) for x in (table, lens, off, acc, num)]
+    for order in ([0, 1, 2], [2, 0, 1]):
+        x = both.clone()
+        pa.pa_cache_compact([x[i, 0] for i in order], [x[i, 1] for i in order], *a)
+        assert np.array_equal(x.view(torch.int16).cpu().numpy(), np.stack(want, 1))
+    with pytest.raises(pa.PaError):
+        pa.pa_cache_compact([both[0, 0], both[0, 0]], [both[0, 1], both[1, 1]], *a)

@@ -215,3 +215,15 @@ def test_truncate_refuses(pa):
     a.seq_truncate(s, 0)
     assert a.block_table([s], 4)[1] == [0] and a.stats()["free"] == 4
     assert pa.lib().pa_seq_truncate(None, 0, 0) == pa.PA_ERR_INVALID
+
+
+# ------------------------------------------------------------------------------ memory that calls may not share
+
+def test_compact_refuses_layers_that_share_memory(pa):
+    """A layer named twice would have its rows moved twice."""
+    size = 10 * 2 * 16 * 64 * 2                                # bytes of a cache of compact_rc's shape
+    ks, vs = [A, A + size], [A + 2 * size, A + 3 * size]
+    for bad in (dict(ks=[A, A]), dict(ks=[A, A + size - 16]), dict(vs=[A + size, A + 4 * size]), dict(ks=vs),
+                dict(ks=[A + 2 * size + 16, A]), dict(n=1, ks=[A], vs=[A])):
+        assert compact_rc(pa, **(dict(ks=ks, vs=vs) | bad)) == pa.PA_ERR_INVALID, bad
+        assert b"share memory" in pa.lib().pa_last_error_string()
