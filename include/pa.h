@@ -549,8 +549,8 @@ int pa_decode_tree(const void* d_q, const void* d_k_cache, const void* d_v_cache
  *   d_accepted           [num_seqs][max_accepted] int32, ascending per sequence
  *                        (a path from a root down is)
  *   d_num_accepted       [num_seqs] int32
- *   d_new_seq_lens       NULL, or [num_seqs] int32, not d_seq_lens itself:
- *                        seq_lens[b] - n_b + num_accepted[b]
+ *   d_new_seq_lens       NULL, or [num_seqs] int32, over none of the arrays
+ *                        above: seq_lens[b] - n_b + num_accepted[b]
  *   d_error_bits         NULL, or as for pa_tree_plan: PA_DEVERR_TREE;
  *                        PA_DEVERR_SEQ_LEN for a bad length or offset (that
  *                        sequence keeps its rows and length);

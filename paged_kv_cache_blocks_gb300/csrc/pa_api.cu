@@ -32,6 +32,13 @@ int fail(int code, const std::string& msg) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + static_cast<uintptr_t>(b_bytes) &&
+         y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 bool supported_head_dim(int32_t d) { return d == 64 || d == 128; }
 
 // An NVTX range around one library call, visible to Nsight tools (no cost
@@ -727,8 +734,15 @@ int pa_cache_compact(void* const* k_caches, void* const* v_caches, int32_t num_l
       !aligned(d_accepted, 4) || !aligned(d_num_accepted, 4) || !aligned(d_new_seq_lens, 4) ||
       !aligned(d_error_bits, 4))
     return fail(PA_ERR_INVALID, "pa_cache_compact: arrays must be aligned to their elements");
-  if (d_new_seq_lens == d_seq_lens)
-    return fail(PA_ERR_INVALID, "pa_cache_compact: new_seq_lens must not be seq_lens");
+  // one thread of a sequence writes its new length while others read its inputs
+  const int64_t lens_bytes = 4 * static_cast<int64_t>(num_seqs);
+  if (d_new_seq_lens &&
+      (overlap(d_new_seq_lens, lens_bytes, d_seq_lens, lens_bytes) ||
+       overlap(d_new_seq_lens, lens_bytes, d_q_offsets, lens_bytes + 4) ||
+       overlap(d_new_seq_lens, lens_bytes, d_accepted, lens_bytes * max_accepted) ||
+       overlap(d_new_seq_lens, lens_bytes, d_num_accepted, lens_bytes)))
+    return fail(PA_ERR_INVALID, "pa_cache_compact: new_seq_lens must not overlap seq_lens, q_offsets, accepted or "
+                                "num_accepted");
   pa::CompactArgs a;
   a.k_caches = k_caches;
   a.v_caches = v_caches;

@@ -227,3 +227,12 @@ def test_compact_refuses_layers_that_share_memory(pa):
                 dict(ks=[A + 2 * size + 16, A]), dict(n=1, ks=[A], vs=[A])):
         assert compact_rc(pa, **(dict(ks=ks, vs=vs) | bad)) == pa.PA_ERR_INVALID, bad
         assert b"share memory" in pa.lib().pa_last_error_string()
+
+
+def test_compact_refuses_new_lengths_over_its_inputs(pa):
+    """They are written by one thread of a sequence while others still read its inputs."""
+    size = 10 * 2 * 16 * 64 * 2
+    ok = dict(ks=[A, A + size], vs=[A + 2 * size, A + 3 * size], lens=A + 256, off=A + 512, acc=A + 1024, num=A + 2048)
+    for new in (ok["lens"] + 4, ok["lens"] - 4, ok["off"] + 8, ok["acc"] + 20, ok["num"], ok["num"] - 4):
+        assert compact_rc(pa, **(ok | dict(new=new))) == pa.PA_ERR_INVALID, new
+        assert b"new_seq_lens" in pa.lib().pa_last_error_string()
