@@ -420,7 +420,8 @@ int pa_prefill(const void* d_q, const void* d_k_cache, const void* d_v_cache, in
  *   d_slot_mapping  as for pa_cache_write; a padding token's (slot < 0) k and
  *                   v are not written, its q is
  *   d_q_out         [num_tokens][num_q_heads][head_dim]; may be d_q itself
- *                   when that is packed, and may not overlap it otherwise
+ *                   when that is packed, and may overlap none of q, k and v
+ *                   otherwise (PA_ERR_INVALID)
  *   caches, num_blocks, dtype  as for pa_cache_write; head_dim 64 or 128, any
  *                   head counts > 0, num_tokens times heads at most 2^30
  *

@@ -485,7 +485,8 @@ def pa_rope_cache_write(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_c
     q [T, Hq, D], k and v [T, Hkv, D]: contiguous heads, any token stride but
     0, so views of one projection's rows do.  positions [T] int32; slot_mapping [T]
     int64 (< 0: padding); inv_freq [rotary_dim / 2] float64; caches
-    [NB, Hkv, 16, D].  ``out`` may be a contiguous q itself.
+    [NB, Hkv, 16, D].  ``out`` may be a contiguous q itself, and may overlap
+    q, k and v in no other way.
     """
     return _rope(lib().pa_rope_cache_write, q, k, v, positions, slot_mapping, inv_freq, (), k_cache, v_cache, out,
                  q_norm, k_norm, eps, interleaved, attn_factor, dtype, stream)

@@ -477,6 +477,17 @@ int rope_common(const char* name, const void* d_q, const void* d_k, const void* 
       !aligned(opts->d_k_norm, 16) || !aligned(d_positions, 4) || !aligned(d_slot_mapping, 8) ||
       !aligned(opts->d_inv_freq, 8) || !aligned(d_k_scale, 4) || !aligned(d_v_scale, 4))
     return bad(PA_ERR_INVALID, "q, k, v, q_out, the norm weights and the caches must be 16-byte aligned");
+  // q_out against rows of `heads` heads, `stride` elements apart
+  const int64_t out_bytes = 2 * static_cast<int64_t>(num_tokens) * num_q_heads * head_dim;
+  auto over = [&](const void* rows, int64_t heads, int64_t stride) {
+    if (stride > INT32_MAX || stride < INT32_MIN) return false;   // refused below
+    const int64_t span = (num_tokens - 1) * stride;
+    return overlap(d_q_out, out_bytes, static_cast<const char*>(rows) + 2 * (span < 0 ? span : 0),
+                   2 * ((span < 0 ? -span : span) + heads * head_dim));
+  };
+  const bool in_place = d_q_out == d_q && (num_tokens == 1 || qs == static_cast<int64_t>(num_q_heads) * head_dim);
+  if ((!in_place && over(d_q, num_q_heads, qs)) || over(d_k, num_kv_heads, ks) || over(d_v, num_kv_heads, vs))
+    return bad(PA_ERR_INVALID, "q_out must be q itself, packed, or overlap none of q, k and v");
   pa::RopeArgs a;
   a.q = d_q;
   a.k = d_k;

@@ -236,3 +236,16 @@ def test_compact_refuses_new_lengths_over_its_inputs(pa):
     for new in (ok["lens"] + 4, ok["lens"] - 4, ok["off"] + 8, ok["acc"] + 20, ok["num"], ok["num"] - 4):
         assert compact_rc(pa, **(ok | dict(new=new))) == pa.PA_ERR_INVALID, new
         assert b"new_seq_lens" in pa.lib().pa_last_error_string()
+
+
+def test_rope_refuses_an_output_over_its_inputs(pa):
+    """q_out is q itself, packed, or apart from q, k and v: other threads still read what it would write."""
+    S = 4 * 8 * 128 * 2                                        # bytes of packed q
+    ok = dict(q=A, k=A + 2 * S, v=A + 3 * S, out=A + 4 * S)
+    row = (8 + 2 + 2) * 128                                    # elements of a projection's row
+    for bad in (dict(out=A + 16), dict(out=A + 2 * S), dict(out=A + 3 * S - 16), dict(out=A + S // 2),
+                dict(out=A, qst=row),                          # q in place, but not packed
+                dict(out=A + 16, q=A + 3 * row * 2 + 32, qst=-row)):
+        for fp8 in (False, True):
+            assert rope_rc(pa, fp8, **(ok | bad)) == pa.PA_ERR_INVALID, bad
+            assert b"q_out" in pa.lib().pa_last_error_string()
