@@ -516,7 +516,7 @@ int pa_tree_plan(const int32_t* d_parents, const int32_t* d_q_offsets, const int
  *                64 * mask_words of a tree are not computed (flagged
  *                PA_DEVERR_SEQ_LEN)
  *   caches, d_block_tables, d_seq_lens, d_q_offsets, max_seq_len, dtype: as for
- *                pa_prefill; scale must be > 0
+ *                pa_prefill; max_seq_len at most 2^31 - 128, scale > 0
  *   d_workspace  >= pa_decode_tree_workspace_bytes(...) bytes, 256-byte
  *                aligned, caller-owned; calls sharing it must not overlap
  *   opts         NULL, or events recorded around the attention kernel

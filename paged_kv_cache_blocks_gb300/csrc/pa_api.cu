@@ -641,6 +641,8 @@ int pa_decode_tree(const void* d_q, const void* d_k_cache, const void* d_v_cache
   if (max_seq_len <= 0) max_seq_len = cap;
   if (max_seq_len > cap)
     return fail(PA_ERR_INVALID, "pa_decode_tree: max_seq_len exceeds max_blocks_per_seq * 16");
+  if (max_seq_len > INT32_MAX - 127)   // a length is rounded up to chunks of 128 keys in 32 bits
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_tree: max_seq_len must be at most 2^31 - 128");
   if (!std::isfinite(scale) || scale <= 0.f)
     return fail(PA_ERR_INVALID, "pa_decode_tree: scale must be finite and > 0");
   if (opts && (opts->variant != 0 || opts->flags != 0 || opts->partition_tokens != 0))

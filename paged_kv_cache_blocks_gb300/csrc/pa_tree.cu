@@ -330,8 +330,9 @@ __global__ void __launch_bounds__(kPlanSeqs) tree_prep_kernel(const TreePrepArgs
       const float cuts = work_f * inv;
       const float even = (mu * work_f + item * (pairs + cuts) + fminf(2.f * cuts, cuts + pairs)) / sms;
       cost = fmaxf(even, mu * size + 2.f * item) + 5.5f;
-      // its cuts fall where they may: only where the slots hold any of them
-      if (cuts + 3.f * pairs > kMaxSlots - 1 || P.num_seqs > nthr) cost = 3e38f;
+      // its cuts fall where they may: only where the slots hold any of them, and
+      // the chunks of all sequences, which it counts through, fit 32 bits
+      if (cuts + 3.f * pairs > kMaxSlots - 1 || P.num_seqs > nthr || s_work > 1ull << 30) cost = 3e38f;
     } else {
       const float each = chunks / fmaxf(large, 1.f), full = fmaxf(ceilf(large / sms) - 1.f, 0.f);
       const float waves = full * mu * each + each * fmaxf(1.f, mu * (large / sms - full)) + (full + 1.f) * item;

@@ -249,3 +249,13 @@ def test_rope_refuses_an_output_over_its_inputs(pa):
         for fp8 in (False, True):
             assert rope_rc(pa, fp8, **(ok | bad)) == pa.PA_ERR_INVALID, bad
             assert b"q_out" in pa.lib().pa_last_error_string()
+
+
+def test_tree_refuses_lengths_that_round_up_past_32_bits(pa):
+    """The kernels count keys in 32 bits, in chunks of 128: the last length that rounds up within them is 2^31 - 128."""
+    most = (1 << 31) - 128
+    for bad in (dict(msl=most + 1), dict(msl=most + 112), dict(msl=0)):
+        assert tree_rc(pa, mb=(1 << 27) - 1, wsb=0, **bad) == pa.PA_ERR_UNSUPPORTED
+        assert b"max_seq_len" in pa.lib().pa_last_error_string()
+    assert tree_rc(pa, mb=(1 << 27) - 1, wsb=0, msl=most) == pa.PA_ERR_INVALID           # past that check, to the workspace's
+    assert b"workspace" in pa.lib().pa_last_error_string()
