@@ -522,9 +522,10 @@ int pa_tree_plan(const int32_t* d_parents, const int32_t* d_q_offsets, const int
  *   opts         NULL, or events recorded around the attention kernel
  *
  * fp32 accumulation, the softmax weights rounded to dtype for the tensor
- * cores, one rounding to dtype at the end.  NaN and infinities in the K or V
- * of a tree token reach only the tokens that see it.  Bad device data is
- * clamped and flagged as by pa_prefill.  Resources as for pa_prefill's
+ * cores (fp16: by half a step, from 2^-21 of the largest down by at most
+ * 2^-32 of it), one rounding to dtype at the end.  NaN and infinities in the
+ * K or V of a tree token reach only the tokens that see it.  Bad device data
+ * is clamped and flagged as by pa_prefill.  Resources as for pa_prefill's
  * tcgen05 kernel. */
 size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
                                       int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);

@@ -712,8 +712,15 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         const float alpha = need ? exp2f(m_ref - new_ref) : 1.f;
         // p = 2^(s * scale - mu) as 16-bit, two per column, into this half's
         // 32 columns of P, once the previous chunk's product over this half
-        // has read them; row sum in fp32 (pairs on the packed two-lane FMA/add)
-        const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(-mu, -mu);
+        // has read them; row sum in fp32 (pairs on the packed two-lane FMA/add).
+        // The tensor cores take P in T, so each weight is rounded once, by half
+        // a step of T; the sum keeps it in fp32.  Trees: an fp16 weight of less
+        // than 2^-14 would be subnormal and lose bits, one of 2^-25 all; as the
+        // weights end at 2^8, kBias puts them 2^7 higher (2^15 < 65504), and
+        // the quotient O / l drops it.
+        constexpr float kBias = kTree && std::is_same<T, __half>::value ? 7.f : 0.f;
+        const float shift = kBias > 0.f ? kBias - mu : -mu;
+        const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(shift, shift);
         float2 r2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[32];
 #pragma unroll

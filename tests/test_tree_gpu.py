@@ -461,3 +461,31 @@ def test_threads_call_at_once(pa):
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("gap", [20.7, 24.4, 26.3])
+@pytest.mark.parametrize("hq,hkv,D,dt", [(4, 2, 64, "f16"), (8, 1, 128, "f16"), (8, 1, 128, "bf16")])
+def test_weights_far_below_the_largest(pa, gap, hq, hkv, D, dt):
+    """Keys whose weight is 2^-gap of the largest and that alone have values: fp16 weights of theirs would be
+    subnormal, or nothing.  Two keys of every 1024 have the largest weight, one in either half of a chunk, and the
+    value 0.  Beside check()'s terms: a stored fp16 weight, 2^7 times its share of the largest, may be off by half a
+    subnormal step, 2^-25, so all of them by keys 2^-32 against a sum of at least the largest weights' number."""
+    r = np.random.default_rng(14)
+    L, n = 8192, 5
+    a = make(r, [L - n], [n], hq, hkv, D, dt, poison=False)
+    k, v = torch.zeros(L, dtype=a["q"].dtype), torch.full((L,), 64, dtype=a["q"].dtype)
+    top = [p for p in range(L - n) if p % 1024 in (0, 64)]
+    k[top], v[top] = gap / (16 * a["scale"] * np.log2(np.e)), 0
+    table = a["block_tables"][0, :L // 16].long()
+    a["q"].zero_()[..., 0] = 16
+    a["k_cache"].zero_()[table, :, :, 0] = k.cuda().view(-1, 1, 16)
+    a["v_cache"][table] = v.cuda().view(-1, 1, 16, 1)
+    out = pa.pa_decode_tree(**a)
+    m = lambda t: t.double().cpu().numpy()
+    want, size, dots = ref.tree_attention(m(a["q"]), m(a["k_cache"]), m(a["v_cache"]), a["block_tables"].cpu().numpy(),
+                                          a["seq_lens"].cpu().numpy(), a["q_offsets"].cpu().numpy(),
+                                          a["masks"].cpu().numpy().view(np.uint64), a["scale"])
+    u, e = torch.finfo(TORCH_DT[dt]).eps / 2, (D + 4) * 2.0 ** -24 * dots[..., None]
+    tol = u * np.abs(want) + (u + 2 * e + 2.0 ** -20 + (L + 64) * 2.0 ** -22) * size * (1 + 2 * u) + 2.0 ** -24
+    tol += 64 * L / len(top) * 2.0 ** -32
+    assert (np.abs(m(out) - want) <= tol).all(), (np.abs(m(out) - want) / tol).max()
