@@ -466,10 +466,17 @@ int pa_rope_cache_write_fp8(const void* d_q, const void* d_k, const void* d_v, c
  *                   the fastest kept ("NTK-aware")
  *   PA_ROPE_RAMP    those that turn beta_fast times or more within
  *                   trained_tokens kept, those that turn beta_slow times or
- *                   less divided by factor, linear between ("YaRN"); its
- *                   *attn_factor_out is 0.1 ln(factor) + 1, else 1
+ *                   less divided by factor, linear in the turns between (the
+ *                   equation of the YaRN paper)
+ *   PA_ROPE_RAMP_INDEX  the same, but linear in i between the indexes where a
+ *                   pair turns beta_fast and beta_slow times, rounded down and
+ *                   up: what checkpoints with a YaRN scaling are served with.
+ *                   Between the ends it differs from PA_ROPE_RAMP, up to
+ *                   twofold
+ * *attn_factor_out is 0.1 ln(factor) + 1 for the ramps, else 1; a model that
+ * ramps its frequencies without scaling its scores passes 1 instead.
  * Arguments that a scaling does not name are not read. */
-enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BASE = 2, PA_ROPE_RAMP = 3 };
+enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BASE = 2, PA_ROPE_RAMP = 3, PA_ROPE_RAMP_INDEX = 4 };
 int pa_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
                         double trained_tokens, double beta_fast, double beta_slow, double* inv_freq_out,
                         float* attn_factor_out);

@@ -414,14 +414,15 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, q_offsets, scale, ma
 
 # --------------------------------------------------------------------------- rotation and draft trees
 
-ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "ramp_index": 4}
 
 
 def pa_rope_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0, trained_tokens=0.0,
                         beta_fast=32.0, beta_slow=1.0, device="cuda"):
     """(inv_freq [rotary_dim / 2] float64 on ``device``, attn_factor) for
     pa_rope_cache_write: plain, or scaled for a longer context ("linear",
-    "base", "ramp"; see pa.h)."""
+    "base", "ramp" linear in a pair's turns, "ramp_index" linear in its index
+    as checkpoints with a YaRN scaling expect; see pa.h)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
     out = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)

@@ -552,30 +552,41 @@ int pa_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double
     return fail(PA_ERR_INVALID, "pa_rope_frequencies: rotary_dim must be even and > 0, the outputs not NULL");
   if (!(base > 1.0) || !std::isfinite(base))
     return fail(PA_ERR_INVALID, "pa_rope_frequencies: base must be finite and > 1");
-  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_RAMP)
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_RAMP_INDEX)
     return fail(PA_ERR_INVALID, "pa_rope_frequencies: unknown scaling");
   if (scaling != PA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
     return fail(PA_ERR_INVALID, "pa_rope_frequencies: factor must be finite and >= 1");
   if (scaling == PA_ROPE_BASE && rotary_dim <= 2)
     return fail(PA_ERR_INVALID, "pa_rope_frequencies: scaling the base needs rotary_dim > 2");
-  if (scaling == PA_ROPE_RAMP && (!(trained_tokens > 0.0) || !(beta_fast > beta_slow) || !(beta_slow > 0.0) ||
-                                  !std::isfinite(trained_tokens) || !std::isfinite(beta_fast)))
+  const bool ramp = scaling == PA_ROPE_RAMP || scaling == PA_ROPE_RAMP_INDEX;
+  if (ramp && (!(trained_tokens > 0.0) || !(beta_fast > beta_slow) || !(beta_slow > 0.0) || !std::isfinite(trained_tokens) ||
+               !std::isfinite(beta_fast)))
     return fail(PA_ERR_INVALID,
                 "pa_rope_frequencies: the ramp needs trained_tokens > 0 and beta_fast > beta_slow > 0");
   const double two_pi = 6.283185307179586476925;
   if (scaling == PA_ROPE_BASE) base *= std::pow(factor, rotary_dim / (rotary_dim - 2.0));
+  // the pair, as a real index, that turns so many times within trained_tokens
+  auto index = [&](double turns) {
+    return 0.5 * rotary_dim * std::log(trained_tokens / (two_pi * turns)) / std::log(base);
+  };
+  double low = 0.0, high = 0.0;
+  if (scaling == PA_ROPE_RAMP_INDEX) {
+    low = std::fmax(std::floor(index(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(index(beta_slow)), rotary_dim - 1.0);
+    if (high <= low) high = low + 0.001;   // a step
+  }
   for (int32_t i = 0; i < rotary_dim / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rotary_dim);
     if (scaling == PA_ROPE_LINEAR) f /= factor;
-    if (scaling == PA_ROPE_RAMP) {
+    if (ramp) {
       const double turns = trained_tokens * f / two_pi;
-      double keep = (turns - beta_slow) / (beta_fast - beta_slow);
+      double keep = scaling == PA_ROPE_RAMP ? (turns - beta_slow) / (beta_fast - beta_slow) : (high - i) / (high - low);
       keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
       f = f * keep + f / factor * (1.0 - keep);
     }
     inv_freq_out[i] = f;
   }
-  *attn_factor_out = scaling == PA_ROPE_RAMP ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+  *attn_factor_out = ramp ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
   return PA_OK;
 }
 

@@ -259,3 +259,30 @@ def test_tree_refuses_lengths_that_round_up_past_32_bits(pa):
         assert b"max_seq_len" in pa.lib().pa_last_error_string()
     assert tree_rc(pa, mb=(1 << 27) - 1, wsb=0, msl=most) == pa.PA_ERR_INVALID           # past that check, to the workspace's
     assert b"workspace" in pa.lib().pa_last_error_string()
+
+
+def test_frequencies_ramped_over_the_pairs(pa):
+    """The ramp that checkpoints of the YaRN scaling are served with: linear in the pair's index, between the indexes
+    (rounded outward) where a pair turns beta_fast and beta_slow times within the trained length."""
+    for r, base, factor, trained, fast, slow in ((128, 1e6, 4.0, 32768, 32, 1), (64, 1e4, 40.0, 4096, 32, 1),
+                                                 (128, 5e5, 8.0, 8192, 32, 1), (16, 1e4, 2.0, 64, 1.2, 1.1),
+                                                 (32, 1e4, 16.0, 10 ** 9, 32, 1), (32, 1e4, 4.0, 10 ** 15, 32, 1), (32, 1e4, 4.0, 2, 32, 1)):
+        y, a = pa.pa_rope_frequencies(r, base, "ramp_index", factor=factor, trained_tokens=trained, beta_fast=fast,
+                                      beta_slow=slow, device="cpu")
+        at = lambda turns: r / 2 * math.log(trained / (2 * math.pi * turns)) / math.log(base)
+        low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), r - 1)
+        if high <= low:
+            high = low + 0.001
+        for i in range(r // 2):
+            f = base ** (-2 * i / r)
+            along = min(max((i - low) / (high - low), 0), 1)
+            assert math.isclose(y[i].item(), f * (1 - along) + f / factor * along, rel_tol=1e-12), (r, i)
+        assert math.isclose(a, 0.1 * math.log(factor) + 1, rel_tol=1e-7)
+    # by hand: base 1e4, 64 values, trained 4096: indexes 10.47 and 22.51, so pairs 0-10 are kept and from 23 on divided
+    y, _ = pa.pa_rope_frequencies(64, 1e4, "ramp_index", factor=40.0, trained_tokens=4096, device="cpu")
+    ratio = y.numpy() * 1e4 ** (np.arange(0, 64, 2) / 64)
+    assert np.allclose(ratio[:11], 1, rtol=1e-12) and np.allclose(ratio[23:], 1 / 40, rtol=1e-12)
+    assert np.allclose(np.diff(ratio[10:24]), -(1 - 1 / 40) / 13, rtol=1e-9)
+    for kw in (dict(), dict(trained_tokens=64, beta_fast=1.0, beta_slow=1.0), dict(trained_tokens=64, factor=0.5)):
+        with pytest.raises(pa.PaError):
+            pa.pa_rope_frequencies(64, scaling="ramp_index", device="cpu", **({"factor": 2.0} | kw))
