@@ -205,3 +205,72 @@ def test_no_tokens_and_all_padding(pa):
     z, size = ref.rope(n64(q), pos.cpu().numpy(), f.cpu().numpy(), False, 1.0)
     assert (np.abs(n64(out) - z) <= bound(z, size, "f16")).all()
     assert torch.equal(kc, k0) and torch.equal(vc, v0)
+
+
+@pytest.mark.parametrize("T", [128, 129, 300, 1000])
+@pytest.mark.parametrize("dt,interleaved,norm", [("bf16", False, True), ("f16", True, True), ("bf16", True, False),
+                                                 ("f16", False, False)])
+def test_e4m3_cache_of_a_long_piece(pa, T, dt, interleaved, norm):
+    """A prompt's piece from within a page on, in pages of any order, with padding inside and at both ends: runs of V
+    rows go over the edges of the groups of tokens that are written together.  Bounds as in test_e4m3_cache."""
+    hq, hkv, D, rotary = 4, 3, 128, 64
+    q, k, v, pos, _, f, _, _ = make(T, hq, hkv, D, dt, 5 * T, True, rotary=rotary)
+    g = torch.Generator().manual_seed(T)
+    pool = T // 16 + 4
+    at = torch.arange(5, 5 + T)
+    slots = torch.randperm(pool, generator=g)[at // 16] * 16 + at % 16
+    gone = torch.tensor([0, 40, 127, T // 2, T - 1])
+    slots[gone] = -1
+    slots[41] = pool * 16                     # outside the pool
+    slots = slots.cuda()
+    kc = torch.randint(0, 0x7F, (pool, hkv, 16, D), generator=g, dtype=torch.uint8).cuda()
+    vc = torch.randint(0, 0x7F, (pool, hkv, D, 16), generator=g, dtype=torch.uint8).cuda()
+    ks, vs = (0.002 + 0.02 * torch.rand(hkv, generator=g)).cuda(), (0.002 + 0.02 * torch.rand(hkv, generator=g)).cuda()
+    w = [(1 + 0.2 * torch.randn(D, generator=g)).to(q.dtype).cuda() for _ in range(2)] if norm else [None, None]
+    wn = [None if x is None else n64(x) for x in w]
+    kc0, k8, v8 = kc.clone(), kc.clone(), vc.clone()
+    out = pa.pa_rope_cache_write_fp8(q, k, v, pos, slots, f, ks, vs, kc, vc, q_norm=w[0], k_norm=w[1], eps=1e-5,
+                                     interleaved=interleaved, attn_factor=1.25)
+    p, fr = pos.cpu().numpy(), f.cpu().numpy()
+    z, size = ref.rope(n64(q), p, fr, interleaved, 1.25, wn[0], 1e-5)
+    assert (np.abs(n64(out) - z) <= bound(z, size, dt)).all()
+    z, size = ref.rope(n64(k), p, fr, interleaved, 1.25, wn[1], 1e-5)
+    s = slots.cpu().numpy()
+    live = (s >= 0) & (s < pool * 16)
+    got = kc.view(torch.float8_e4m3fn).float().double().cpu().numpy()[s[live] // 16, :, s[live] % 16]
+    scale = n64(ks)[:, None]
+    x = np.clip(z[live] / scale, -448, 448)
+    assert (np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -10 + 2.0 ** -15 * size[live] / scale).all()
+    same = np.ones((pool, 16), bool)
+    same[s[live] // 16, s[live] % 16] = False
+    assert torch.equal(kc.transpose(1, 2)[torch.from_numpy(same).cuda()], kc0.transpose(1, 2)[torch.from_numpy(same).cuda()])
+    # v, and k where nothing turns or norms it: the codes of pa_cache_write_fp8, the rows around them as they were
+    pa.pa_cache_write_fp8(k.contiguous(), v.contiguous(), slots, ks, vs, k8, v8)
+    assert torch.equal(v8, vc) and (norm or torch.equal(k8[..., rotary:], kc[..., rotary:]))
+
+
+@pytest.mark.parametrize("position", [12345, 1000003, 2 ** 31 - 1, -(2 ** 31) + 5])
+def test_far_angles_near_the_zeros_of_sine_and_cosine(pa, position):
+    """q = (1, 0) turns into (cos t, sin t); the frequencies put t close to a zero of one of them, where fp16 resolves
+    2^-24.  The frequency is held as a 64-bit fraction of a turn, off by 2 units at most; the angle is cut to 32 bits
+    of a turn, and then rounded to fp32, which moves it by pi 2^-25 near a quarter turn and not at all near 0."""
+    from fractions import Fraction
+    r = np.random.default_rng(abs(position))
+    two_pi = Fraction(6283185307179586476925286766559005768, 10 ** 36)
+    quarter = np.arange(64) % 2               # odd pairs: a quarter of a turn further
+    near = r.uniform(1e-5, 1e-4, 64) * r.choice([-1, 1], 64)
+    turns = (r.uniform(0.001, 0.25, 64) * abs(position)).astype(np.int64) + quarter * 0.25
+    f = torch.tensor((turns * 2 * np.pi + near) / abs(position), dtype=torch.float64)
+    q = torch.cat([torch.ones(64), torch.zeros(64)]).half().view(1, 1, 128).cuda()
+    kc = torch.zeros(1, 1, 16, 128, dtype=torch.float16, device="cuda")
+    out = pa.pa_rope_cache_write(q, q, q, torch.tensor([position], dtype=torch.int32).cuda(),
+                                 torch.tensor([3]).cuda(), f.cuda(), kc, kc.clone())
+    got = n64(out)[0, 0]
+    for i in range(64):
+        t = Fraction(f[i].item()) * position / two_pi
+        t = float((t - round(t)) * two_pi)
+        exact = np.sin(t) if not quarter[i] else np.cos(t)
+        assert abs(exact) < 2e-4, t
+        tol = 2.0 ** -25 + 2 * np.pi * (2.0 ** -32 + abs(position) * 2.0 ** -63) + 2.0 ** -21 * abs(exact)
+        assert abs(got[64 + i if not quarter[i] else i] - exact) <= tol + quarter[i] * np.pi * 2.0 ** -25, i
+    assert torch.equal(kc[0, 0, 3], out[0, 0])

@@ -489,3 +489,17 @@ def test_weights_far_below_the_largest(pa, gap, hq, hkv, D, dt):
     tol = u * np.abs(want) + (u + 2 * e + 2.0 ** -20 + (L + 64) * 2.0 ** -22) * size * (1 + 2 * u) + 2.0 ** -24
     tol += 64 * L / len(top) * 2.0 ** -32
     assert (np.abs(m(out) - want) <= tol).all(), (np.abs(m(out) - want) / tol).max()
+
+
+def test_many_sequences_some_of_them_split(pa):
+    """More than the plan holds at a time, long ones among the first and among the others."""
+    r = np.random.default_rng(15)
+    befores, sizes = r.integers(0, 150, 1100), r.integers(0, 3, 1100)
+    befores[[3, 1050]], sizes[[3, 1050]] = [30000, 17000], [3, 2]
+    a = make(r, befores.tolist(), sizes.tolist(), 4, 4, 64, "bf16", poison=False)
+    a["block_tables"] = a["block_tables"].contiguous()
+    w = ws(pa, a, a["block_tables"].shape[1] * 16)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    out = pa.pa_decode_tree(**a, workspace=w, events=events)
+    assert pa.pa_decode_check(w) == 0 and events[0].elapsed_time(events[1]) > 0
+    check(a, out, "bf16")
