@@ -158,8 +158,8 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
 //               shared to tensor memory; per chunk it reads its 64 scores,
 //               applies the scale and the causal mask, runs an online softmax
 //               in fp32 with its own running maximum (moved only when it
-//               grows by more than 2^8: the exact result either way, fewer
-//               rescales of its O), scale-and-subtract and row sums on the
+//               grows by more than 2^8, fp16 trees 2^4: the exact result either
+//               way, fewer rescales of its O), scale-and-subtract and row sums on the
 //               packed two-lane fp32 FMA / add, and writes its P as 16-bit
 //               values, two per column.  The halves never wait for each other
 //               inside an item; at its end they exchange (maximum, sum) and
@@ -537,6 +537,13 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
     const int row = 32 * quarter + lane;
     const uint32_t lane_addr = tbase + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t o_mine = lane_addr + C::kColO + D * half;
+    // The running maximum moves when it grows by more than 2^kGrow.  Trees: an
+    // fp16 weight of less than 2^-14 would be subnormal and lose bits, one of
+    // 2^-25 all, so the weights are stored 2^kBias higher and the quotient
+    // O / l drops it.  With kGrow 4 they end at 2^11: the 2^5 below fp16's
+    // largest hold what the rounding of a maximum up to 2^26 can add.
+    constexpr bool kLift = kTree && std::is_same<T, __half>::value;
+    constexpr float kBias = kLift ? 7.f : 0.f, kGrow = kLift ? 4.f : 8.f;
     uint32_t it = 0, cc = 0, xk = 0;
     bool ok = true;
     auto wait = [&](int idx, uint32_t parity) {
@@ -706,7 +713,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], t[i]);
         // the scale is positive, so it commutes with the maximum
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * P.scale_log2;
-        const bool need = mx > m_ref + 8.f;
+        const bool need = mx > m_ref + kGrow;
         const float new_ref = need ? mx : m_ref;
         const float mu = new_ref == -INFINITY ? 0.f : new_ref;
         const float alpha = need ? exp2f(m_ref - new_ref) : 1.f;
@@ -714,12 +721,8 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         // 32 columns of P, once the previous chunk's product over this half
         // has read them; row sum in fp32 (pairs on the packed two-lane FMA/add).
         // The tensor cores take P in T, so each weight is rounded once, by half
-        // a step of T; the sum keeps it in fp32.  Trees: an fp16 weight of less
-        // than 2^-14 would be subnormal and lose bits, one of 2^-25 all; as the
-        // weights end at 2^8, kBias puts them 2^7 higher (2^15 < 65504), and
-        // the quotient O / l drops it.
-        constexpr float kBias = kTree && std::is_same<T, __half>::value ? 7.f : 0.f;
-        const float shift = kBias > 0.f ? kBias - mu : -mu;
+        // a step of T; the sum keeps it in fp32.
+        const float shift = kLift ? kBias - mu : -mu;
         const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(shift, shift);
         float2 r2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[32];

@@ -503,3 +503,20 @@ def test_many_sequences_some_of_them_split(pa):
     out = pa.pa_decode_tree(**a, workspace=w, events=events)
     assert pa.pa_decode_check(w) == 0 and events[0].elapsed_time(events[1]) > 0
     check(a, out, "bf16")
+
+
+def test_fp16_scores_of_tens_of_millions_stay_finite(pa):
+    """The maximum of such scores is rounded by whole units, so a weight may exceed what the reference allows for by
+    some powers of two.  All values are 1: so is the result, but for a rounding each of the weights and the output."""
+    a = make(np.random.default_rng(16), [380], [4], 8, 1, 128, "f16", poison=False)
+    table = a["block_tables"][0, :24].long()
+    for first in (7880, 7096, 4000):
+        for second in (48, 64, 80):
+            k = torch.zeros(24 * 16, 128, dtype=torch.float16)
+            k[:, 0] = first
+            k[128:256, 1], k[256:, 1] = second, 2 * second
+            a["q"].zero_()[..., :2] = torch.tensor([60000.0, 1.0])
+            a["k_cache"][table] = k.cuda().view(24, 1, 16, 128)
+            a["v_cache"].fill_(1)
+            out = pa.pa_decode_tree(**a)
+            assert (out.double() - 1).abs().max() <= 2.0 ** -10 + 2.0 ** -20, (first, second)
