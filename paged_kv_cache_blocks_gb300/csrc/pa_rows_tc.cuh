@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
       mbar_init(&bar[B::kPFull + i], C::kSoftmaxWarps / 2);   // per key half
       mbar_init(&bar[B::kODone + i], 1);
       mbar_init(&bar[B::kItemFull + i], 1);
-      // helpers (3), MMA issuers (2), softmax (4)
+      // the other producers (3), MMA issuers (2), softmax (8)
       mbar_init(&bar[B::kItemEmpty + i], C::kProducerWarps - 1 + C::kMmaWarps + C::kSoftmaxWarps);
     }
     mbar_init(&bar[B::kQFull], 1);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
   if (warp >= C::kProducerWarp0 && warp < C::kMmaWarp) {
     // ------------------------------------------------------------ producers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsProducer));
-    // Warp 4 takes items from the atomic counter and publishes them; all
+    // Warp 8 takes items from the atomic counter and publishes them; all
     // four producer warps read block ids 32 at a time (one coalesced load)
     // and each issues the copies of blocks p and p + 4 of every chunk
     // (lanes 0..3: block p / p + 4, dims 0-63 / 64-127), arming the stage
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
     }
   } else if (warp >= C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers
-    // lane 0 of warp 8 issues the S products, lane 0 of warp 9 the PV
+    // lane 0 of warp 12 issues the S products, lane 0 of warp 13 the PV
     // products: issuing blocks a thread about as long as the product runs,
     // so with one issuer its waits and commits sat between the products;
     // with two, each one's bookkeeping overlaps the other's products
