@@ -1175,7 +1175,7 @@ TRAFFIC = {
     ("cow", "auto"): {"bytes": 268.53e6 + 216.54e6, "kernel_src": "52affb2a945dc192",
                       "profile": "profiles/copy_blocks_kernel_cow.md"},
     # the 8 prefill launches of one step (iterations 1..8), summed
-    ("chunked", "auto"): {"bytes": 1285.85e6 + 286.66e6, "kernel_src": "aefb1ffede7ea4be",
+    ("chunked", "auto"): {"bytes": 1287.25e6 + 290.13e6, "kernel_src": "cdc2b66f9a06f49e",
                           "profile": "profiles/prefill_tc_kernel_chunked.md"},
 }
 

@@ -16,7 +16,7 @@ namespace pa {
 // sequence move, so the chain of loads (lengths and accepted tokens, page ids,
 // rows) bounds it: it is walked once for several layers, as many as leave
 // about three CTAs for every SM.  32 layers, 64 sequences, 4 moves each at the
-// 8B shape: 14.9 us for 67 MB (batches of 8 at two CTAs an SM 16.7; a chain per
+// 8B shape: 14 to 15 us for 67 MB (batches of 8 at two CTAs an SM 16.7; a chain per
 // layer 18.6).
 constexpr int kSms = 152;             // for the choice of a CTA's share only
 constexpr int kCompactLayers = 128;   // layers of one launch (their pointers are kernel arguments)

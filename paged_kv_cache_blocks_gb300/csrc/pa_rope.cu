@@ -27,7 +27,9 @@
 // token's values 16 bytes apart: CTAs of their own take kVTokens consecutive
 // tokens of a head, quantise them into shared memory and write each run of
 // tokens that fills a page's 16 rows with one 16-byte store per dimension; the
-// rest (a page's beginning or end, single tokens) byte by byte.
+// rest (a page's beginning or end, single tokens) byte by byte.  30000 tokens,
+// 1168 MB: 195 us in runs of pages (0.88 of the copy rate), 260 us scattered;
+// 256 single tokens 12.6 us (16-bit caches 4.1).
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -51,7 +53,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 // Rows a thread: they share the CTA's angles and index arithmetic, against the
 // registers that keep four CTAs on an SM.  us for 3770 tokens at the 70B shape /
-// 30000 to E4M3 / 256 tokens: 2 rows 26.0 / 210 / 4.2, 3 rows 24.7 / 201 / 4.1,
+// 30000 to E4M3 in runs of pages / 256 tokens: 2 rows 26.0 / 210 / 4.2, 3 rows 24.7 / 201 / 4.1,
 // 4 rows 25.1 / 212 / 4.1 (25.5 / 208 with three CTAs an SM).
 constexpr int kRopeRows = 3;
 
@@ -87,7 +89,7 @@ __device__ __forceinline__ uint64_t turn_fraction(double w) {
   return w < 0 ? 0 - f : f;
 }
 
-constexpr int kVTokens = 128;   // us for 30000 tokens: 32 tokens 215, 64 202, 128 198
+constexpr int kVTokens = 128;   // us for 30000 tokens in runs of pages: 32 tokens 215, 64 202, 128 198
 
 // V rows of kVTokens tokens from t0 on, head h, into the E4M3 cache.
 template <typename T>

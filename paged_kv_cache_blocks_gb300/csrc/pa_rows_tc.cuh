@@ -158,14 +158,14 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
 //               shared to tensor memory; per chunk it reads its 64 scores,
 //               applies the scale and the causal mask, runs an online softmax
 //               in fp32 with its own running maximum (moved only when it
-//               grows by more than 2^8, fp16 trees 2^4: the exact result either
-//               way, fewer rescales of its O), scale-and-subtract and row sums on the
-//               packed two-lane fp32 FMA / add, and writes its P as 16-bit
-//               values, two per column.  The halves never wait for each other
+//               grows by more than 2^8, fp16 trees 2^4: the exact result
+//               either way, fewer rescales of its O), scale-and-subtract and
+//               row sums on the packed two-lane fp32 FMA / add, and writes its
+//               P as 16-bit values, two per column.  The halves never wait for each other
 //               inside an item; at its end they exchange (maximum, sum) and
 //               each writes 64 dims of (O0 2^(m0-m) + O1 2^(m1-m)) / l.
 // The softmax warpgroups take registers the producer warpgroup gives back
-// (setmaxnreg), so that nothing spills.
+// (setmaxnreg), so that nothing spills (in the trees' kernels three words).
 // For trees an item is short (its epilogue 1.2 to 2.3 us against 0.9 to 1.4 us a
 // chunk), so its end overlaps the next one's start: the softmax warps fetch the
 // next record and move the next Q before they wait for the last product, and

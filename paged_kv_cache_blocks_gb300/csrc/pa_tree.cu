@@ -24,7 +24,7 @@
 //   4 short chats, trees of 5, head_dim 64                     10.8
 //   64 sequences of 128-2048 tokens, trees of 1-32, 32/8 heads 64    307 MB  0.71
 //   256 sequences, a tenth of 34,000 tokens, trees of 1-8      548   3781 MB 1.02
-//   8 x 32,768 tokens, trees of 64 (256 rows)                  227   1084 MB, 275 GFLOP 0.64
+//   8 x 32,768 tokens, trees of 64 (256 rows)                  228   1084 MB, 275 GFLOP 0.63
 // The second spends 4 us in the plan, 4 before its first scores, 47 streaming
 // pages (7 TB/s) and up to 6 in CTAs whose last items are short; the last's
 // pace is that of the kernel's softmax (0.9 us per 128 x 128 scores an SM).
