@@ -211,3 +211,20 @@ def test_layers_in_any_order_and_interleaved(pa):
         assert np.array_equal(x.view(torch.int16).cpu().numpy(), np.stack(want, 1))
     with pytest.raises(pa.PaError):
         pa.pa_cache_compact([both[0, 0], both[0, 0]], [both[0, 1], both[1, 1]], *a)
+
+
+def test_pages_past_4_gib(pa):
+    """The moved rows in the last pages of pools of 5 GiB."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB of device memory")
+    c, table, lens, off, acc, num = make(9, [20, 33], [9, 30], [5, 12], 1, 8, 128, "bf16")
+    want, want_lens = ref.compact(c, table, lens, off, acc, num)
+    far = (5 << 30) // (8 * 16 * 128 * 2)
+    pool = c[0].shape[1]
+    big = [torch.zeros(1, far + pool, 8, 16, 128, dtype=torch.int16, device="cuda") for _ in range(2)]
+    for x, y in zip(big, c):
+        x[:, far:] = torch.from_numpy(y).cuda()
+    new = pa.pa_cache_compact(*big, dev(np.where(table < 0, table, table + far)), dev(lens), dev(off), dev(acc), dev(num))
+    assert np.array_equal(new.cpu().numpy(), want_lens)
+    for x, y in zip(big, want):
+        assert np.array_equal(x[:, far:].cpu().numpy(), y) and not x[:, :far].any()

@@ -274,3 +274,30 @@ def test_far_angles_near_the_zeros_of_sine_and_cosine(pa, position):
         tol = 2.0 ** -25 + 2 * np.pi * (2.0 ** -32 + abs(position) * 2.0 ** -63) + 2.0 ** -21 * abs(exact)
         assert abs(got[64 + i if not quarter[i] else i] - exact) <= tol + quarter[i] * np.pi * 2.0 ** -25, i
     assert torch.equal(kc[0, 0, 3], out[0, 0])
+
+
+def test_pages_past_4_gib(pa):
+    """The last pages of pools of 5 GiB: the same rows as in a small pool, and nothing at their offsets modulo 2^32."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of device memory")
+    T, hq, hkv = 40, 8, 8
+    q, k, v, pos, slots, f, kc, vc = make(T, hq, hkv, 128, "bf16", 31, True, pool=12)
+    page = hkv * 16 * 128 * 2
+    far = (5 << 30) // page
+    big = [torch.zeros(far + 12, hkv, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kc.zero_(), vc.zero_()
+    want = pa.pa_rope_cache_write(q, k, v, pos, slots, f, kc, vc)
+    got = pa.pa_rope_cache_write(q, k, v, pos, slots + far * 16, f, *big)
+    assert torch.equal(got, want)
+    for x, y in zip(big, (kc, vc)):
+        assert torch.equal(x[far:], y)
+        assert not x[:far].view(torch.int16).any()
+    del big, x
+    ks, vs = (torch.full((hkv,), 0.02, device="cuda") for _ in range(2))
+    k8, v8 = torch.zeros(12, hkv, 16, 128, dtype=torch.uint8, device="cuda"), torch.zeros(12, hkv, 128, 16, dtype=torch.uint8, device="cuda")
+    far *= 2
+    b8 = [torch.zeros(far + 12, *x.shape[1:], dtype=torch.uint8, device="cuda") for x in (k8, v8)]
+    pa.pa_rope_cache_write_fp8(q, k, v, pos, slots, f, ks, vs, k8, v8)
+    pa.pa_rope_cache_write_fp8(q, k, v, pos, slots + far * 16, f, ks, vs, *b8)
+    for x, y in zip(b8, (k8, v8)):
+        assert torch.equal(x[far:], y) and not x[:far].any()

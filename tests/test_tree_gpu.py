@@ -520,3 +520,42 @@ def test_fp16_scores_of_tens_of_millions_stay_finite(pa):
             a["v_cache"].fill_(1)
             out = pa.pa_decode_tree(**a)
             assert (out.double() - 1).abs().max() <= 2.0 ** -10 + 2.0 ** -20, (first, second)
+
+
+def test_rows_of_no_tree(pa):
+    """A captured batch whose sequences have no drafts this time: nothing is written, nothing flagged."""
+    a = make(np.random.default_rng(17), [100, 30, 0], [3, 2, 1], 8, 2, 128, "bf16")
+    a["q_offsets"].zero_()
+    w = ws(pa, a, a["block_tables"].shape[1] * 16)
+    out = torch.full_like(a["q"], 5.0)
+    pa.pa_decode_tree(**a, workspace=w, out=out)
+    assert pa.pa_decode_check(w) == 0 and (out == 5.0).all()
+    err = torch.zeros(1, dtype=torch.int32).cuda()
+    masks, pos = torch.full((6, 1), 7).cuda(), torch.full((6,), 8, dtype=torch.int32).cuda()
+    pa.pa_tree_plan(torch.full((6,), -1, dtype=torch.int32).cuda(), a["q_offsets"], a["seq_lens"], masks=masks,
+                    positions=pos, error_bits=err)
+    assert (masks == 7).all() and (pos == 8).all() and err.item() == 0
+
+
+def test_two_graphs_at_once(pa):
+    """Replayed on two streams together, each with a workspace of its own."""
+    r = np.random.default_rng(18)
+    cases = [make(r, [3000, 10, 700], [16, 8, 40], 8, 1, 128, "bf16", poison=False) for _ in range(2)]
+    graphs, outs, want = [], [], []
+    for a in cases:
+        w, out, g = ws(pa, a, a["block_tables"].shape[1] * 16), torch.empty_like(a["q"]), torch.cuda.CUDAGraph()
+        want.append(pa.pa_decode_tree(**a, workspace=w))
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                pa.pa_decode_tree(**a, workspace=w, out=out)
+        graphs.append(g), outs.append((out, w))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (out, w), x in zip(outs, want):
+        assert torch.equal(out, x) and pa.pa_decode_check(w) == 0
